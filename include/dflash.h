@@ -411,8 +411,11 @@ int dflash_rope_append_kv(const dflash_append_params* p, const void* q, const vo
  *                      e4m3(code), v likewise.  Every scale of a page that
  *                      holds a visible key is finite and > 0, and the value
  *                      scales of one request and kv head lie within a factor
- *                      of 2^64 of each other; scales of other pages are not
- *                      read.
+ *                      of 2^100 of each other, so that slots of zeros, which
+ *                      dflash_rope_append_kv gives 2^-100, may stand beside
+ *                      ordinary ones (values below 2^-64 of others' size may
+ *                      come out larger, up to that 2^-64); scales of other
+ *                      pages are not read.
  * Other arguments, masks (window, future_keys, right_window), outputs, device
  * status and return codes as dflash_block_attn.  The codes enter the tensor
  * cores as they are: q as the sum of two E4M3 terms (exact for elements down to

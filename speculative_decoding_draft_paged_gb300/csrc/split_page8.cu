@@ -7,11 +7,16 @@
 //   x_rj = sum_d q_rd kc_jd          (kc, vc: the stored codes)
 //   s_rj = scale log2(e) ks_j x_rj   (ks, vs: the page's scales)
 //   lse2_r = log2 sum_j 2^s_rj,      out_r = sum_j 2^(s_rj - lse2_r) vs_j vc_j.
-// With t_rj = s_rj + log2(vs_j) and a bias n_r per row such that t_rj + n_r <= 8
-// the sums the kernel keeps are
-//   O_rd = sum_j P_rj vc_jd,  l_r = sum_j P_rj / vs_j,  P_rj = 2^(t_rj + n_r),
-// so out = O / l and lse2 = log2(l) - n: the value scale rides in the
-// exponent and costs no product per key.
+// With ws_j = vs_j / vs_0 (vs_0: the scale of the unit's first page),
+// t_rj = s_rj + log2(ws_j) and a bias n_r per row such that t_rj + n_r <= 8 the
+// sums the kernel keeps are
+//   O_rd = sum_j P_rj vc_jd,  l_r = sum_j P_rj / ws_j,  P_rj = 2^(t_rj + n_r),
+// so out = vs_0 O / l and lse2 = log2(l) - n: the value scale rides in the
+// exponent and costs no product per key.  Taken relative to vs_0, a cache whose
+// scales are all near 2^-100 (values of zero) stays in the middle of fp32's
+// range.  ws_j is held at 2^-64 or more: a page that quiet adds nothing to sums
+// that the first one's scale is part of, and 1 / ws_j cannot overflow l.  Upwards
+// it may reach 2^100: keys 2^-32 of a row's largest are still in l.
 //
 // bf16 factors on fp8 operands.  A bf16 value has 8 significant bits, an E4M3
 // code 4: q (times one power of two per tile, which puts the tile's largest
@@ -75,6 +80,7 @@ constexpr int kP8T = 128;                // keys per tile
 constexpr float kP8First = 3.f;          // a row's largest P is 2^3 when its bias is first set,
 constexpr float kP8Off = 4.5f;           // 2^4.5 when it moves,
 constexpr float kP8Limit = 8.f;          // and may grow to 2^8 before that
+constexpr float kP8Quietest = -64.f;     // least log2 of a value scale over the first page's
 
 // Tile and row groups, CTAs per SM and ring stages by head dim and padded rows.
 // Measured, one side against the other:
@@ -300,7 +306,8 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
   volatile int* issued_v = reinterpret_cast<volatile int*>(misc + 3);
   uint32_t* q_amax = misc + 4;                                            // largest |q| of the tile, as bits
   volatile int* stop_word = reinterpret_cast<volatile int*>(misc + 8);    // [TG NG], set by a group's own warps
-  float4* scale_ring = reinterpret_cast<float4*>(gbase + C::kOffScale);   // (ks, log2 vs, 1/vs) per page of a tile
+  volatile float* first_lv = reinterpret_cast<volatile float*>(misc + 12);  // log2 vs_0, set by the K producer
+  float4* scale_ring = reinterpret_cast<float4*>(gbase + C::kOffScale);   // (ks, log2 ws, 1/ws) per page of a tile
   float* rows = reinterpret_cast<float*>(gbase + C::kOffRow);             // per tile group: n_r,
   float* const row_bias = rows;                                           //
   float* const row_set = rows + TG * RP;                                  // 0: no key seen yet,
@@ -403,6 +410,7 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
     };
     if (!is_v) ask_scales(pg_cur);
     float4 sc_cur;
+    float lv0 = 0.f;  // log2 vs_0
     const uint64_t kv_policy = l2_policy_evict_first();
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     const int ns = is_v ? NSV : NSK;
@@ -438,7 +446,14 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
         // completed, waited for the scores of tile j - NSK - NB to be read.
         if (lane0 == 0) {
           const float lv = log2f(vs_nxt);
-          sc_cur = make_float4(ks_nxt, lv, exp2f(-lv), 0.f);
+          if (j == 0) {  // the first page that holds a visible key
+            const unsigned have = __ballot_sync(0xffffffffu, pg_cur >= 0);
+            lv0 = have != 0 ? __shfl_sync(0xffffffffu, lv, __ffs(have) - 1) : 0.f;
+            if (lane == 0) *first_lv = lv0;
+          }
+          float rel = pg_cur >= 0 ? lv - lv0 : 0.f;
+          if (rel < kP8Quietest) rel = kP8Quietest;
+          sc_cur = make_float4(ks_nxt, rel, exp2f(-rel), 0.f);
         } else if (lane0 == ppt) {
           ask_scales(pg_nxt);
         }
@@ -628,7 +643,7 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
       tc_fence_after();
       uint32_t x[NR];
       load_scores<NR>(lane_addr + buf * RP + row0, x);
-      // y = t + n.  The page's log2 vs joins each row's bias in registers: put
+      // y = t + n.  The page's log2 ws joins each row's bias in registers: put
       // together in shared memory, one lane a row, it took 2 to 4 % longer (64/4
       // window 99.1 against 95.2 us, 64/16 ragged 607 against 599).
       const float4 sc = scale_ring[entry * 8 + page_of_key];
@@ -811,7 +826,7 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
           sum = sums[g] != 0.f ? fmaf(f, sums[g], sum) : sum;
         }
 #pragma unroll
-        for (int g = 0; g < TG; ++g) row_fac[g * RP + r] *= sum != 0.f ? 1.f / sum : 0.f;
+        for (int g = 0; g < TG; ++g) row_fac[g * RP + r] *= sum != 0.f ? exp2f(*first_lv) / sum : 0.f;
         if (r < a.R) {
           const float lse = sum > 0.f ? log2f(sum) - least : p8_ninf();
           // Where the row lies in the output, from the first of the block's rows.
