@@ -23,11 +23,15 @@
 // magnitude in [2^7, 2^8)) is hi + lo with both terms E4M3, exactly down to
 // 2^-10 of the largest value and to 2^-18 of it below; both terms accumulate
 // into the same scores.  P is hi + lo / 32: hi is P rounded to 4 bits, lo the
-// rest times 32, rounded to 4 bits, so P keeps a relative 2^-9 (bf16: 2^-8)
-// down to 2^-6, and 2^-15 below; the two terms accumulate apart and join in
-// the epilogue.  A row's largest P lies in [2^3, 2^8], so what is lost below
-// is 2^-18 of it; the factor 32 is what keeps the tail of a long context with
-// one dominant key from flushing to zero.
+// rest times 32, rounded to 4 bits, so P keeps a relative 2^-8.7 (with its step
+// through f16) down to 2^-6, and 2^-15 below; the two terms accumulate apart and join in
+// the epilogue.  Only the tile at hand has to fit that range: O and l are fp32
+// and are rescaled when the bias moves, down for a key louder than all before
+// and up again for the tail behind it, which would otherwise flush to zero (with
+// 131072 keys behind one of 0.9 of the weight and a value of zero, all of the
+// output; now 0.2 % of it).  What stays lost are keys that share a tile with a
+// far louder one: below 2^-23 of it where it stands alone, else 2^-19, so at most
+// 127 times that of a row's weight each time.
 //
 // Transposed products, keys along M:
 //   S^T [128 keys x RP rows] = K [128 x D] (K-major, as TMA lands it) Q^T,
@@ -37,10 +41,11 @@
 // TMEM lane) and RP / NG rows: the scales are per-thread scalars, the mask is
 // a row interval, and P goes to shared memory as 16-byte pieces.  What the
 // threads of a row must share is the bias n_r: it is set from the row's
-// largest t in its first tile (to P = 2^3, which leaves scores five bits to
-// grow) and moves only when a P would pass 2^8 (then O and l are rescaled),
-// which the group's four warps agree on by one barrier per tile that also
-// carries the vote.
+// largest t in its first tile (to P = 2^4, which leaves scores four bits to
+// grow) and moves when a P would pass 2^8, which the group's four warps agree
+// on by one barrier per tile that also carries the vote, or when a look at the
+// tile's column maxima (the second tile, every 16th, and the one behind a large
+// step down) finds a row below 2^-5.
 //
 // Grid (splits, Hkv, B), one unit of C 128-key tiles per CTA, as the mma.sync
 // kernel; the combine kernel merges the units.
@@ -77,9 +82,28 @@ namespace dflash {
 namespace {
 
 constexpr int kP8T = 128;                // keys per tile
-constexpr float kP8First = 3.f;          // a row's largest P is 2^3 when its bias is first set,
-constexpr float kP8Off = 4.5f;           // 2^4.5 when it moves,
-constexpr float kP8Limit = 8.f;          // and may grow to 2^8 before that
+// A row's bias.  When it is first set and when it moves, its tile's largest P is
+// put to 2^kP8Set, or to 2^kP8Limit where that of 32 keys lies kP8Alone above
+// those of the other 96, in the first tile or with a step as large (a key that
+// stands alone is not soon passed, and what shares its tile keeps four bits
+// more).  A P past 2^kP8Limit moves it, and with it every row of the group above
+// 2^kP8Off.  Looks (the second tile, every kP8Every-th but the last few, the one
+// behind a step down of kP8Drop or more) move rows whose tile stays below
+// 2^kP8Low, but never more than kP8Rise above the lowest bias the row had: 2^17
+// keys 2^-32 below the loudest weigh 2^-15 of it.
+// Measured, 64/4 heads of 128 with a window of 4096 / 12/2 heads of 64 at 128K, 7
+// tokens, scores of deviation 1 (and 3): only falling, first at 2^3, 98 (125) /
+// 268 (303) us, but the tail lost; these values 103 (138) / 274 (358).  A look
+// every 32nd tile 102 / 272, every 8th 105 / 275; kP8Drop at -8 (148) / (390);
+// only rows past 2^kP8Limit moved 117 / 283.
+constexpr float kP8Limit = 8.f;
+constexpr float kP8Set = 4.f;
+constexpr float kP8Off = 4.5f;
+constexpr float kP8Alone = 6.f;
+constexpr float kP8Low = -5.f;
+constexpr float kP8Rise = 32.f;
+constexpr float kP8Drop = -10.f;
+constexpr int kP8Every = 16;
 constexpr float kP8Quietest = -64.f;     // least log2 of a value scale over the first page's
 
 // Tile and row groups, CTAs per SM and ring stages by head dim and padded rows.
@@ -128,7 +152,7 @@ struct P8Cfg {
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffScale = kOffMisc + 64;              // float4 [kRing][8]
   static constexpr int kOffRow = kOffScale + kRing * 8 * 16;
-  // float [TG][RP] each: bias, set, delta, fac; then colmax [TG][4][RP]
+  // float [TG][RP] each: bias, cap, delta, fac; then colmax [TG][4][RP]
   static constexpr int kSmem = kOffRow + 8 * TG * RP * 4 + 1024;
   static constexpr int kColO = NB * RP;  // tensor memory: NB score buffers of RP columns, TG accumulators of kPCols
   static constexpr int kCols = kColO + TG * kPCols;
@@ -310,7 +334,7 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
   float4* scale_ring = reinterpret_cast<float4*>(gbase + C::kOffScale);   // (ks, log2 ws, 1/ws) per page of a tile
   float* rows = reinterpret_cast<float*>(gbase + C::kOffRow);             // per tile group: n_r,
   float* const row_bias = rows;                                           //
-  float* const row_set = rows + TG * RP;                                  // 0: no key seen yet,
+  float* const row_cap = rows + TG * RP;                                  // the highest it may rise to (+inf: no key seen yet),
   float* const row_delta = rows + 2 * TG * RP;                            // a moving bias's step and
   float* const row_fac = rows + 3 * TG * RP;                              // factor; the output factor in the end
   float* const colmax = rows + 4 * TG * RP;                               // [TG][4][RP]
@@ -385,7 +409,7 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
   }
   for (int r = threadIdx.x; r < TG * RP; r += C::kThreads) {
     row_bias[r] = 0.f;
-    row_set[r] = 0.f;
+    row_cap[r] = -p8_ninf();
   }
   tc_fence_before();
   __syncthreads();  // barriers, row state and the TMEM address are visible
@@ -555,7 +579,7 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
     const int bar_id = 1 + (warp >> 2);    // the group's barrier; 15 joins all softmax warps
     const int row0 = grp * NR;             // the group's first row
     float* const my_bias = row_bias + tg * RP + row0;
-    float* const my_set = row_set + tg * RP + row0;
+    float* const my_cap = row_cap + tg * RP + row0;
     float* const my_delta = row_delta + tg * RP + row0;
     float* const my_fac = row_fac + tg * RP + row0;
     float* const my_colmax = colmax + tg * 4 * RP + row0;
@@ -620,7 +644,8 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
 #pragma unroll
     for (int r = 0; r < NR; ++r) l[r] = 0.f;
 
-    bool bad = false;  // a wait of this warp ran out
+    bool dropped = false;  // a bias fell far with the last tile
+    bool bad = false;      // a wait of this warp ran out
     auto failed = [&]() {
       bad = true;
       stop_word[warp >> 2] = 1;
@@ -697,10 +722,11 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
           for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(vrow + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      // The group's first tile sets the biases; so does its second where a
-      // row's window starts behind the first.
-      const bool set = k == 0 || (k == 1 && lo_all >= p0 - (TG - 1) * T);
-      if (barrier_any(bar_id, 128, fmaxf(mx, mx1) > kP8Limit || set || bad)) {
+      // The group's first tile sets the biases, its second those of rows whose
+      // window starts behind the first.
+      const bool look = k <= 1 || dropped || (k % kP8Every == 0 && n - j > kP8Every / 2);
+      dropped = false;
+      if (barrier_any(bar_id, 128, fmaxf(mx, mx1) > kP8Limit || look || bad)) {
         if (stop_word[warp >> 2] != 0) break;
         // ---- new biases.  Column maxima over the tile's keys, per warp.
 #pragma unroll
@@ -709,63 +735,66 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
           if (lane == 0) *reinterpret_cast<float4*>(my_colmax + quad * RP + r) = m;
         }
         named_barrier(bar_id, 128);
+        float delta = 0.f;
         if (gthread < NR) {
           const int r = gthread;
-          const float M = fmaxf(fmaxf(my_colmax[r], my_colmax[RP + r]), fmaxf(my_colmax[2 * RP + r], my_colmax[3 * RP + r]));
+          const float m0 = my_colmax[r], m1 = my_colmax[RP + r], m2 = my_colmax[2 * RP + r], m3 = my_colmax[3 * RP + r];
+          const float a01 = fmaxf(m0, m1), a23 = fmaxf(m2, m3);
           // M = the tile's largest t + n; -inf when the row sees no key of it.
-          const float old = my_bias[r];
-          float delta = 0.f, fac = 1.f;
-          if (my_set[r] == 0.f) {
-            if (M != p8_ninf()) {  // O and l of the row are zero so far
-              delta = kP8First - M;
-              my_set[r] = 1.f;
-            }
-          } else if (M > kP8Off) {
-            delta = kP8Off - M;
-            fac = fast_exp2(delta);
+          const float M = fmaxf(a01, a23);
+          const float second = fmaxf(fminf(a01, a23), fmaxf(fminf(m0, m1), fminf(m2, m3)));  // the largest of the other warps
+          const float old = my_bias[r], cap = my_cap[r];
+          const bool first = cap == -p8_ninf();  // O and l of the row are zero so far
+          if (M > p8_ninf() && (first || M > kP8Off || (look && M < kP8Low))) {
+            const bool alone = M - second > kP8Alone && (first || M > kP8Limit + kP8Alone);
+            const float now = fminf(old + ((alone ? kP8Limit : kP8Set) - M), cap);
+            delta = now - old;
+            my_bias[r] = now;
+            my_cap[r] = fminf(cap, now + kP8Rise);
           }
-          my_bias[r] = old + delta;
           my_delta[r] = delta;
-          my_fac[r] = fac;
+          my_fac[r] = first ? 1.f : fast_exp2(delta);
         }
-        named_barrier(bar_id, 128);
+        if (barrier_any(bar_id, 128, delta != 0.f)) {
 #pragma unroll
-        for (int q = 0; q < NR / 4; ++q) {
-          const float4 dl = reinterpret_cast<const float4*>(my_delta)[q];
-          const float4 fc = reinterpret_cast<const float4*>(my_fac)[q];
-          y[4 * q] += dl.x;
-          y[4 * q + 1] += dl.y;
-          y[4 * q + 2] += dl.z;
-          y[4 * q + 3] += dl.w;
-          l[4 * q] *= fc.x;
-          l[4 * q + 1] *= fc.y;
-          l[4 * q + 2] *= fc.z;
-          l[4 * q + 3] *= fc.w;
-        }
-        if (k > 0) {
-          // O holds the group's earlier tiles once their PV has completed.
-          if (!wait_warp(pv_done(tg + TG * ((k - 1) & 1)), ((k - 1) >> 1) & 1)) failed();
-          tc_fence_after();
-#pragma unroll 1
-          for (int e8 = 0; e8 < NR; e8 += 8) {
-            const float4 f0 = *reinterpret_cast<const float4*>(my_fac + e8), f1 = *reinterpret_cast<const float4*>(my_fac + e8 + 4);
-            const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-            float least = f[0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) least = fminf(least, f[e]);
-            if (least == 1.f) continue;  // (factors are at most 1) alike for every thread of the group
-            uint32_t o0[8], o1[8];
-            tmem_ld8x2_wait(o_addr + 2 * e8, o_addr + 2 * e8 + 8, o0, o1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              o0[e] = __float_as_uint(__uint_as_float(o0[e]) * f[e]);
-              o1[e] = __float_as_uint(__uint_as_float(o1[e]) * f[e]);
-            }
-            tmem_st8(o_addr + 2 * e8, o0);
-            tmem_st8(o_addr + 2 * e8 + 8, o1);
+          for (int q = 0; q < NR / 4; ++q) {
+            const float4 dl = reinterpret_cast<const float4*>(my_delta)[q];
+            const float4 fc = reinterpret_cast<const float4*>(my_fac)[q];
+            y[4 * q] += dl.x;
+            y[4 * q + 1] += dl.y;
+            y[4 * q + 2] += dl.z;
+            y[4 * q + 3] += dl.w;
+            l[4 * q] *= fc.x;
+            l[4 * q + 1] *= fc.y;
+            l[4 * q + 2] *= fc.z;
+            l[4 * q + 3] *= fc.w;
+            dropped = dropped || fminf(fminf(dl.x, dl.y), fminf(dl.z, dl.w)) < kP8Drop;
           }
-          tmem_wait_st();
-          tc_fence_before();
+          if (k > 0) {
+            // O holds the group's earlier tiles once their PV has completed.
+            if (!wait_warp(pv_done(tg + TG * ((k - 1) & 1)), ((k - 1) >> 1) & 1)) failed();
+            tc_fence_after();
+#pragma unroll 1
+            for (int e8 = 0; e8 < NR; e8 += 8) {
+              const float4 f0 = *reinterpret_cast<const float4*>(my_fac + e8), f1 = *reinterpret_cast<const float4*>(my_fac + e8 + 4);
+              const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+              bool rest = true;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) rest = rest && f[e] == 1.f;
+              if (rest) continue;  // alike for every thread of the group
+              uint32_t o0[8], o1[8];
+              tmem_ld8x2_wait(o_addr + 2 * e8, o_addr + 2 * e8 + 8, o0, o1);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                o0[e] = __float_as_uint(__uint_as_float(o0[e]) * f[e]);
+                o1[e] = __float_as_uint(__uint_as_float(o1[e]) * f[e]);
+              }
+              tmem_st8(o_addr + 2 * e8, o0);
+              tmem_st8(o_addr + 2 * e8 + 8, o1);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
         }
       }
       uint8_t* pbuf = gbase + C::kOffP + buf * C::kP;
