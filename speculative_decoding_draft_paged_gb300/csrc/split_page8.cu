@@ -696,7 +696,8 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
         // Rows [ra, ra + len) see this key: those whose last key is not
         // before it, and whose window reaches it.
         int ra = max(0, pos - L - a.rw) * a.G, rb = a.K * a.G;
-        if (a.W > 0) rb = min(a.K, pos + a.W - L) * a.G;
+        // (Compared first: the sum of a large window and the key's place passes 32 bits.)
+        if (a.W > 0 && pos - L < a.K - a.W) rb = (pos - L + a.W) * a.G;
         if (pos >= L + a.K) rb = 0;
         const int len = max(rb - ra, 0);
         ra -= row0;

@@ -1,5 +1,5 @@
-"""Page-scale attention at the ends of its arguments' ranges: pages of zeros
-and value scales far apart."""
+"""Page-scale attention at the ends of its arguments' ranges: windows near
+2^31, pages of zeros and value scales far apart."""
 
 import pytest
 import torch
@@ -9,6 +9,19 @@ from tests._page8 import make_attn
 from tests.test_page_scales_gpu import call, compare
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 100, 2 ** 30 + 1, 308])
+@pytest.mark.parametrize("future_keys,right_window", [(1, 0), (0, 0), (0, 2)])
+@pytest.mark.parametrize("D,Hq", [(128, 16), (64, 4)])
+def test_windows_that_reach_every_key(cuda_device, window, future_keys, right_window, D, Hq):
+    """A window as long as the context or longer masks nothing, up to the
+    largest number its field holds."""
+    inp = make_attn(lens=[0, 1, 100, 120, 128, 300], Hq=Hq, Hkv=1, D=D, K=7, P=32, seed=21)
+    kw = dict(W=window, future_keys=future_keys, right_window=right_window)
+    got = call(inp, cuda_device, **kw)
+    assert got[2] == 0
+    compare(inp, got, **kw)
 
 
 @pytest.mark.parametrize("D,K,Hq", [(64, 1, 4), (64, 7, 4), (64, 7, 6), (128, 7, 16)])
