@@ -420,12 +420,14 @@ int dflash_rope_append_kv(const dflash_append_params* p, const void* q, const vo
  * status and return codes as dflash_block_attn.  The codes enter the tensor
  * cores as they are: q as the sum of two E4M3 terms (exact for elements down to
  * 2^-10 of the largest magnitude of the request's and kv head's queries, to
- * 2^-18 of it below), the probabilities (times their value scales) as the sum of
- * two E4M3 terms under a power of two that follows each row's keys: relative
- * 2^-8.7 down to 2^-10 of the loudest key, off by at most 2^-19 of it, each,
- * below, until the power has followed the row down to a quieter tail (within 16
- * tiles of 128 keys at the latest); a long tail behind dominant keys keeps its
- * share.  The output is divided by the sum of the unrounded probabilities.  Sums,
+ * 2^-18 of it below; rows whose largest lies more than 2^6 to 2^7 below that are
+ * taken in a further pass among themselves, which costs as much time again), the
+ * probabilities (times their value scales) as the sum of two E4M3 terms under a
+ * power of two that follows each row's keys: relative 2^-8.7 down to 2^-10 of the
+ * loudest key, off by at most 2^-19 of it, each, below, until the power has
+ * followed the row down to a quieter tail (within 40 tiles of 128 keys at the
+ * latest); a long tail behind dominant keys keeps its share.  The output is
+ * divided by the sum of the unrounded probabilities.  Sums,
  * maxima and the LSE in fp32.  A NaN in a query, or the NaN code in a key that
  * the row sees, gives a NaN output row with an LSE of -inf; the NaN code in a
  * value that some row of the block sees, NaN outputs in that column of every

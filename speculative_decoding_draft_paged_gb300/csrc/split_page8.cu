@@ -22,16 +22,25 @@
 // code 4: q (times one power of two per tile, which puts the tile's largest
 // magnitude in [2^7, 2^8)) is hi + lo with both terms E4M3, exactly down to
 // 2^-10 of the largest value and to 2^-18 of it below; both terms accumulate
-// into the same scores.  P is hi + lo / 32: hi is P rounded to 4 bits, lo the
-// rest times 32, rounded to 4 bits, so P keeps a relative 2^-8.7 (with its step
-// through f16) down to 2^-6, and 2^-15 below; the two terms accumulate apart and join in
-// the epilogue.  Only the tile at hand has to fit that range: O and l are fp32
-// and are rescaled when the bias moves, down for a key louder than all before
-// and up again for the tail behind it, which would otherwise flush to zero (with
-// 131072 keys behind one of 0.9 of the weight and a value of zero, all of the
-// output; now 0.2 % of it).  What stays lost are keys that share a tile with a
-// far louder one: below 2^-23 of it where it stands alone, else 2^-19, so at most
-// 127 times that of a row's weight each time.
+// into the same scores.  Rows far below the loudest (a quiet head, or all others
+// beside a padding token of any size) would lose theirs: where the largest
+// elements of rows lie more than kP8Apart powers of two apart, the unit is taken
+// again for the quieter ones, under their own power, until none is left.  (At a
+// distance g the scores of a row are off by about 2^(g - 18) of their deviation,
+// so at 6 by 2^-12.  The further pass costs a unit's whole time again, and every
+// other call 0 to 3 %: 64/4 window 102.5 -> 105.8 us.  A power for each row within
+// one pass: 107.8.)
+//
+// P is hi + lo / 32: hi is P rounded to 4 bits, lo the rest times 32, rounded to 4
+// bits, so P keeps a relative 2^-8.7 (with its step through f16) down to 2^-6,
+// and 2^-15 below; the two terms accumulate apart and join in the epilogue.  Only
+// the tile at hand has to fit that range: O and l are fp32 and are rescaled when
+// the bias moves, down for a key louder than all before and up again for the tail
+// behind it, which would otherwise flush to zero (with 131072 keys behind one of
+// 0.9 of the weight and a value of zero, all of the output; now 0.2 % of it).
+// What stays lost are keys that share a tile with a far louder one: below 2^-23
+// of it where it stands alone, else 2^-19, so at most 127 times that of a row's
+// weight each time.
 //
 // Transposed products, keys along M:
 //   S^T [128 keys x RP rows] = K [128 x D] (K-major, as TMA lands it) Q^T,
@@ -105,6 +114,8 @@ constexpr float kP8Rise = 32.f;
 constexpr float kP8Drop = -10.f;
 constexpr int kP8Every = 16;
 constexpr float kP8Quietest = -64.f;     // least log2 of a value scale over the first page's
+enum : uint8_t { kRowTaken, kRowPutOff, kRowDone };  // of a pass over the unit
+constexpr uint32_t kP8Apart = 6;         // powers of two between the largest queries of rows taken together
 
 // Tile and row groups, CTAs per SM and ring stages by head dim and padded rows.
 // Measured, one side against the other:
@@ -153,7 +164,8 @@ struct P8Cfg {
   static constexpr int kOffScale = kOffMisc + 64;              // float4 [kRing][8]
   static constexpr int kOffRow = kOffScale + kRing * 8 * 16;
   // float [TG][RP] each: bias, cap, delta, fac; then colmax [TG][4][RP]
-  static constexpr int kSmem = kOffRow + 8 * TG * RP * 4 + 1024;
+  static constexpr int kOffState = kOffRow + 8 * TG * RP * 4;  // uint8 [RP]
+  static constexpr int kSmem = kOffState + RP + 1024;
   static constexpr int kColO = NB * RP;  // tensor memory: NB score buffers of RP columns, TG accumulators of kPCols
   static constexpr int kCols = kColO + TG * kPCols;
   static constexpr int kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
@@ -181,6 +193,10 @@ __device__ __forceinline__ bool barrier_any(int id, int count, bool p) {
       : "r"(p ? 1 : 0), "r"(id), "r"(count)
       : "memory");
   return any != 0;
+}
+
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // mbar_wait_warp, cheaper where the phase has usually completed.
@@ -281,10 +297,12 @@ __device__ __forceinline__ void split_q2(float a, float b, uint32_t& hi, uint32_
   lo = l;
 }
 
-template <int D, int RP>
-__global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
-    split_page8_kernel(const AttnArgs a, const float* __restrict__ k_scales, const float* __restrict__ v_scales,
-                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+// One pass of a CTA over its unit, for the query rows that lie near the loudest
+// of those not yet done.  Returns whether rows are left for another pass (alike
+// in every thread).  RERUN: not the first.
+template <int D, int RP, bool RERUN>
+__device__ __forceinline__ bool unit_pass(const AttnArgs& a, const float* __restrict__ k_scales, const float* __restrict__ v_scales,
+                                          const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
   using C = P8Cfg<D, RP>;
   constexpr int T = kP8T;
   constexpr int NR = C::NR;
@@ -300,9 +318,9 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
   const int b = blockIdx.z;
   const int L_raw = __ldg(&a.ctx_lens[b]);
   const Geometry geo = make_geometry(L_raw, a.max_ctx_len, a.K, a.W, T, a.C);
-  if (threadIdx.x == 0 && s == 0 && h == 0 && (L_raw < 0 || L_raw > a.max_ctx_len))
+  if (!RERUN && threadIdx.x == 0 && s == 0 && h == 0 && (L_raw < 0 || L_raw > a.max_ctx_len))
     flag_status(a.status, DFLASH_STATUS_BAD_CTX_LEN);
-  if (s >= geo.n_splits) return;  // empty split unit (uniform over the CTA)
+  if (s >= geo.n_splits) return false;  // empty split unit (uniform over the CTA)
   const int tile0 = geo.t_begin + s * a.C;
   const int n = min(geo.n_tiles - s * a.C, a.C);
 
@@ -328,7 +346,8 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile int* issued_k = reinterpret_cast<volatile int*>(misc + 2);
   volatile int* issued_v = reinterpret_cast<volatile int*>(misc + 3);
-  uint32_t* q_amax = misc + 4;                                            // largest |q| of the tile, as bits
+  uint32_t* q_amax = misc + 4;                                            // largest |q| of the rows taken, as bits
+  volatile uint32_t* q_rest = misc + 5;                                   // 1: some rows lie far below it
   volatile int* stop_word = reinterpret_cast<volatile int*>(misc + 8);    // [TG NG], set by a group's own warps
   volatile float* first_lv = reinterpret_cast<volatile float*>(misc + 12);  // log2 vs_0, set by the K producer
   float4* scale_ring = reinterpret_cast<float4*>(gbase + C::kOffScale);   // (ks, log2 ws, 1/ws) per page of a tile
@@ -338,6 +357,7 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
   float* const row_delta = rows + 2 * TG * RP;                            // a moving bias's step and
   float* const row_fac = rows + 3 * TG * RP;                              // factor; the output factor in the end
   float* const colmax = rows + 4 * TG * RP;                               // [TG][4][RP]
+  uint8_t* const row_state = gbase + C::kOffState;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -378,6 +398,8 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
     pg_first = chunk_page(0);
   }
   if (threadIdx.x == C::kThreads - 32) {  // the PV issuer's first lane
+    if constexpr (RERUN)
+      for (int e = 0; e < C::kNumBars; ++e) mbar_inval(bars + 8u * e);
     for (int st = 0; st < NSK; ++st) {
       mbar_init(k_full(st), 1);
       mbar_init(k_empty(st), 1);
@@ -399,17 +421,19 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
     *issued_v = 0;
     for (int g = 0; g < TG * NG; ++g) stop_word[g] = 0;
     *q_amax = 0;
+    *q_rest = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (warp == C::kSoftWarps + 2) {
+  if (warp == C::kSoftWarps + 2 && !RERUN) {
     tmem_alloc(smem_u32(misc), C::kTmem);
     tmem_relinquish();
   }
   for (int r = threadIdx.x; r < TG * RP; r += C::kThreads) {
     row_bias[r] = 0.f;
     row_cap[r] = -p8_ninf();
+    if (r < RP && !RERUN) row_state[r] = kRowTaken;
   }
   tc_fence_before();
   __syncthreads();  // barriers, row state and the TMEM address are visible
@@ -588,22 +612,56 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
     // pieces become codes.
     float inv_qs;
     {
-      uint32_t mx = 0;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      // Largest finite |q| of a piece, and of its row (pieces in neighbouring
+      // lanes), as bits.
+      auto piece_top = [&](int i) -> uint32_t {
         const uint32_t w[4] = {piece[i].x, piece[i].y, piece[i].z, piece[i].w};
+        uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
-          mx = max(mx, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));  // finite values only
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
         }
+        return top;
+      };
+      auto row_top = [&](int i) -> uint32_t {
+        uint32_t top = piece_top(i);
+#pragma unroll
+        for (int m = CPR / 2; m >= 1; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+        return top;
+      };
+      if constexpr (RERUN) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int r = (threadIdx.x + i * kSoft) / CPR;
+          if (r < RP && row_state[r] == kRowDone) piece[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      uint32_t mx = 0, least = 0xffffu;  // least: of the pieces that are not zero
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const uint32_t top = piece_top(i);
+        mx = max(mx, top);
+        least = min(least, top - 1u);
       }
       mx = __reduce_max_sync(0xffffffffu, mx);
       if (lane == 0) atomicMax(q_amax, mx);
       named_barrier(15, kSoft);
-      const int eq = min(261 - static_cast<int>(*reinterpret_cast<volatile uint32_t*>(q_amax) >> 7), 253);
+      const uint32_t most = *reinterpret_cast<volatile uint32_t*>(q_amax) >> 7;
+      const int eq = min(261 - static_cast<int>(most), 253);
       const float qs = __int_as_float(eq << 23);
       inv_qs = __int_as_float((254 - eq) << 23);
+      // Rows far below: seldom a piece, more seldom its row.
+      if (__any_sync(0xffffffffu, ((least + 1) >> 7) + kP8Apart < most)) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const uint32_t top = row_top(i);
+          if (top != 0 && (top >> 7) + kP8Apart < most) {
+            row_state[(threadIdx.x + i * kSoft) / CPR] = kRowPutOff;
+            *q_rest = 1;
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int idx = threadIdx.x + i * kSoft;
@@ -857,9 +915,12 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
         }
 #pragma unroll
         for (int g = 0; g < TG; ++g) row_fac[g * RP + r] *= sum != 0.f ? exp2f(*first_lv) / sum : 0.f;
-        if (r < a.R) {
+        const bool taken = r < a.R && row_state[r] == kRowTaken;
+        if (!taken) row_delta[r] = __int_as_float(-1);
+        if (taken) {
           const float lse = sum > 0.f ? log2f(sum) - least : p8_ninf();
-          // Where the row lies in the output, from the first of the block's rows.
+          // Where the row lies in the output, from the first of the block's rows
+          // (-1: no row, or one of another pass).
           const int i = (r * g_inv) >> 16, place = i * a.Hq + r - i * a.G;
           row_delta[r] = __int_as_float(place);
           // A row that met a NaN: its partial outputs are NaN, and this
@@ -893,10 +954,10 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
         if (D == 128 || lane < 16) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int r = e0 + e;
-            if (r < a.R) {
+            const int r = e0 + e, place = __float_as_int(row_delta[r]);
+            if (place >= 0) {
               if (direct)
-                out[static_cast<size_t>(__float_as_int(row_delta[r])) * D + d] = static_cast<uint16_t>(pack_bf16x2(v[e], 0.f) & 0xffffu);
+                out[static_cast<size_t>(place) * D + d] = static_cast<uint16_t>(pack_bf16x2(v[e], 0.f) & 0xffffu);
               else
                 a.part_o[(unit * a.R + r) * D + d] = v[e];
             }
@@ -913,11 +974,46 @@ __global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
     for (int j = ik > NSK ? ik - NSK : 0; j < ik; ++j) (void)mbar_wait(k_full(j % NSK), (j / NSK) & 1);
     for (int j = iv > NSV ? iv - NSV : 0; j < iv; ++j) (void)mbar_wait(v_full(j % NSV), (j / NSV) & 1);
   }
+  if (*q_rest && !*abort_flag) {
+    // Rows far below the loudest: the unit again, for them alone, once nothing
+    // is left in flight on a barrier.
+    bool ok = true;
+    if (threadIdx.x == 0) {
+      for (int j = max(0, n - NSK); ok && j < n; ++j) ok = mbar_wait(k_empty(j % NSK), (j / NSK) & 1);
+      for (int j = max(0, n - NSV); ok && j < n; ++j) ok = mbar_wait(v_empty(j % NSV), (j / NSV) & 1);
+      for (int j = max(0, n - NB); ok && j < n; ++j)
+        ok = mbar_wait(s_full(j % NB), (j / NB) & 1) && mbar_wait(pv_done(j % NB), (j / NB) & 1);
+      if (!ok) flag_status(a.status, DFLASH_STATUS_TIMEOUT);
+    }
+    if (threadIdx.x < RP) {
+      const uint8_t st = row_state[threadIdx.x];
+      row_state[threadIdx.x] = st == kRowPutOff ? kRowTaken : kRowDone;
+    }
+    if (__syncthreads_and(ok)) return true;
+  }
   __syncthreads();
   if (warp == C::kSoftWarps + 2) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
+  return false;
+}
+
+// The further passes.  As a function of its own: as a loop around the first pass
+// it costs that pass its registers (64/4 window 138 us).
+template <int D, int RP>
+__device__ __noinline__ void later_passes(const AttnArgs& a, const float* k_scales, const float* v_scales,
+                                          const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
+  while (unit_pass<D, RP, true>(a, k_scales, v_scales, tm_k, tm_v)) {
+  }
+}
+
+template <int D, int RP>
+__global__ void __launch_bounds__(P8Cfg<D, RP>::kThreads, P8Cfg<D, RP>::kCtas)
+    split_page8_kernel(const __grid_constant__ AttnArgs a, const float* __restrict__ k_scales,
+                       const float* __restrict__ v_scales, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v) {
+  if (unit_pass<D, RP, false>(a, k_scales, v_scales, tm_k, tm_v)) later_passes<D, RP>(a, k_scales, v_scales, tm_k, tm_v);
 }
 
 template <int D, int RP>
