@@ -336,7 +336,7 @@ int dflash_block_attn_fp8_context_timed(const dflash_params* p, const void* q, c
  * of tokens per request, from a single one to a whole prompt.
  */
 typedef struct dflash_append_params {
-  int32_t batch;             /* B >= 1 requests */
+  int32_t batch;             /* B in 1 .. 2^30 requests */
   int32_t total_tokens;      /* T in 1 .. 2^30: rows of q, k_new, v_new and q_out */
   int32_t num_q_heads;       /* Hq of q (ignored without q) */
   int32_t num_kv_heads;      /* Hkv in 1 .. 32767 */

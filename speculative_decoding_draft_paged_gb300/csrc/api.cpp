@@ -461,7 +461,8 @@ bool append_params_valid(const dflash_append_params* p, bool has_q, bool ragged)
   if (p == nullptr) return false;
   for (int r : p->reserved)
     if (r != 0) return false;
-  if (p->batch < 1 || p->total_tokens < 1 || p->total_tokens > (1 << 30)) return false;
+  // Places in cu_tokens are 32-bit on the device, as are sums of B and T here.
+  if (p->batch < 1 || p->batch > (1 << 30) || p->total_tokens < 1 || p->total_tokens > (1 << 30)) return false;
   if (!ragged && (p->total_tokens % p->batch != 0 || p->total_tokens / p->batch > p->max_new_tokens)) return false;
   if (p->max_new_tokens < 1 || p->max_new_tokens > p->total_tokens) return false;
   if (p->num_kv_heads < 1 || p->num_kv_heads > 32767) return false;
