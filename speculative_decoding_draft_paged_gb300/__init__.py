@@ -654,8 +654,11 @@ def rope_append_kv(q, k_new, v_new, cos_sin, k_pages, v_pages, page_table, ctx_l
             1 if interleaved else 0, positions, 0, 0, q_stride, k_stride, v_stride))
     except struct.error as e:
         raise ValueError(f"an argument does not fit its 32 bits: {e}") from None
-    if workspace is not None and workspace.get_device() != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the current device is cuda:{dev}")
+    if workspace is not None:
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, the current device is cuda:{dev}")
+        if not workspace.is_contiguous() or workspace.nbytes < 4:
+            raise ValueError("workspace must be contiguous and hold the status word's 4 bytes")
     rc = rope_append_kv_raw(p, qp, k_new.data_ptr(), v_new.data_ptr(), cs, k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
                             page_table.data_ptr(), ctx_lens.data_ptr(), cu, op,
                             None if workspace is None else workspace.data_ptr(),

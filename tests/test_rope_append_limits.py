@@ -1,6 +1,7 @@
 """Refusals of the rotating append that need no GPU: nothing is launched."""
 
 import pytest
+import torch
 
 from tests.test_page_scales_abi import append_params
 
@@ -15,3 +16,34 @@ def test_batches_whose_search_would_pass_32_bits(dflash_lib):
         for total in (1, 28, 1 << 30):
             p = append_params(d, batch=batch, total_tokens=total, max_new_tokens=1)
             assert d.rope_append_kv_raw(p, *ptrs) == d.DFLASH_ERR_INVALID
+
+
+@pytest.fixture
+def unlaunched(dflash_lib, monkeypatch):
+    """The Python layer with CPU tensors taken for the current device's, and
+    the library's call replaced: the arguments it would get."""
+    calls = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(dflash_lib, "rope_append_kv_raw", lambda *args: calls.append(args) or 0)
+    types = dflash_lib._types()
+    monkeypatch.setattr(dflash_lib, "_types", lambda: types[:-1] + (lambda device: 0,))
+    return calls
+
+
+def cache(rows, B=2):
+    pages = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
+    return dict(args=(None, rows, rows, None, pages, pages.clone(), torch.zeros(B, 4, dtype=torch.int32),
+                      torch.zeros(B, dtype=torch.int32)), kw=dict(max_ctx_len=32))
+
+
+def test_workspaces_that_do_not_hold_the_status_word(dflash_lib, unlaunched):
+    d = dflash_lib
+    c = cache(torch.zeros(2, 2, 64, dtype=torch.bfloat16))
+    good = torch.zeros(256, dtype=torch.uint8)
+    d.rope_append_kv(*c["args"], **c["kw"], workspace=good)
+    d.rope_append_kv(*c["args"], **c["kw"], workspace=good[:4])
+    assert [args[13] for args in unlaunched] == [good.data_ptr()] * 2
+    for bad in (good[:0], good[:3], torch.zeros(1, dtype=torch.uint8).expand(256), good[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            d.rope_append_kv(*c["args"], **c["kw"], workspace=bad)
+    assert len(unlaunched) == 2
