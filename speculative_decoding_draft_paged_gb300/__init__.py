@@ -560,8 +560,9 @@ def rope_append_kv_raw(p: AppendParams, q_ptr, k_ptr, v_ptr, cos_sin_ptr, k_page
                                              vs_ptr, table_ptr, lens_ptr, cu_ptr, q_out_ptr, ws_ptr, stream_handle)
 
 
-def _token_rows(name, t, H, D, bf16, device):
-    """``[T, H, D]`` (token stride free) or contiguous ``[B, K, H, D]`` rows -> T and the token stride."""
+def _token_rows(name, t, H, D, bf16, device, batch):
+    """``[T, H, D]`` (token stride free) or contiguous ``[B, K, H, D]`` rows (of
+    ``batch`` requests, where it is not None) -> T and the token stride."""
     if t.dim() == 3 and t.dtype in bf16 and t.get_device() == device:
         T, heads, width = t.shape
         row, head, one = t.stride()
@@ -569,6 +570,8 @@ def _token_rows(name, t, H, D, bf16, device):
             return T, row if T > 1 else H * D
     if t.dim() == 4:
         _require(name, t, bf16, (None, None, H, D), device)
+        if batch is not None and t.shape[0] != batch:
+            raise ValueError(f"{name} has rows of {t.shape[0]} requests, ctx_lens has {batch}")
         return t.shape[0] * t.shape[1], t.shape[2] * t.shape[3]
     _require(name, t, bf16, (None, H, D), device, contiguous=False)
     raise ValueError(f"{name}: only the token stride may differ from a packed [T, H, D]")
@@ -582,7 +585,8 @@ def rope_append_kv(q, k_new, v_new, cos_sin, k_pages, v_pages, page_table, ctx_l
 
     ``q`` (or None) ``[T,Hq,D]``, ``k_new``/``v_new [T,Hkv,D]`` bf16, each with
     its own token stride (parts of one projection's output, say), or
-    contiguous ``[B,K,H,D]``.  ``cos_sin [num_positions, r]`` fp32: per
+    contiguous ``[B,K,H,D]`` (B the requests of ``ctx_lens``; with
+    ``cu_tokens`` just B K packed rows).  ``cos_sin [num_positions, r]`` fp32: per
     position the cosines of its r/2 angles, then their sines (None: no
     rotation).  ``page_table [B,max_pages]``, ``ctx_lens [B]`` int32: tokens of
     request b go behind its ``ctx_lens[b]`` cached ones.  ``cu_tokens [B+1]``
@@ -612,12 +616,13 @@ def rope_append_kv(q, k_new, v_new, cos_sin, k_pages, v_pages, page_table, ctx_l
     width = page_table.shape[1]
     _require("page_table", page_table, i32, (B, width), dev)
     _require("ctx_lens", ctx_lens, i32, (B,), dev)
-    T, k_stride = _token_rows("k_new", k_new, Hkv, D, bf16, dev)
-    Tv, v_stride = _token_rows("v_new", v_new, Hkv, D, bf16, dev)
+    batch = B if cu_tokens is None else None
+    T, k_stride = _token_rows("k_new", k_new, Hkv, D, bf16, dev, batch)
+    Tv, v_stride = _token_rows("v_new", v_new, Hkv, D, bf16, dev, batch)
     Hq, q_stride, Tq = 0, 0, T
     if q is not None:
         Hq = q.shape[-2]
-        Tq, q_stride = _token_rows("q", q, Hq, D, bf16, dev)
+        Tq, q_stride = _token_rows("q", q, Hq, D, bf16, dev, batch)
     if Tv != T or Tq != T:
         raise ValueError(f"k_new has {T} tokens, v_new {Tv}, q {Tq}")
     cu = None

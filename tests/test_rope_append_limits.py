@@ -47,3 +47,30 @@ def test_workspaces_that_do_not_hold_the_status_word(dflash_lib, unlaunched):
         with pytest.raises(ValueError, match="workspace"):
             d.rope_append_kv(*c["args"], **c["kw"], workspace=bad)
     assert len(unlaunched) == 2
+
+
+def test_rows_by_request_name_the_batch(dflash_lib, unlaunched):
+    """[B, K, H, D] rows carry their batch: one that is not ctx_lens' would be
+    split among the requests in another way."""
+    d = dflash_lib
+    rows = torch.zeros(6, 4, 2, 64, dtype=torch.bfloat16)
+    q = torch.zeros(6, 4, 3, 64, dtype=torch.bfloat16)
+    c = cache(rows, B=6)
+    assert d.rope_append_kv(q, *c["args"][1:], **c["kw"]).shape == q.shape
+    p = unlaunched[0][0]
+    assert (p.batch, p.total_tokens, p.max_new_tokens) == (6, 24, 4)
+    for B in (2, 3, 8, 12):
+        c = cache(rows, B=B)
+        with pytest.raises(ValueError, match="requests"):
+            d.rope_append_kv(*c["args"], **c["kw"])
+    c = cache(rows.view(24, 2, 64), B=6)
+    for wrong in (q.view(4, 6, 3, 64), q.view(3, 8, 3, 64)):
+        with pytest.raises(ValueError, match="requests"):
+            d.rope_append_kv(wrong, *c["args"][1:], **c["kw"])
+    # With cu_tokens the rows are packed, whatever their first two sizes.
+    cu = torch.tensor([0, 5, 24], dtype=torch.int32)
+    c = cache(rows, B=2)
+    d.rope_append_kv(*c["args"], **c["kw"], cu_tokens=cu, max_new_tokens=19)
+    p = unlaunched[1][0]
+    assert (p.batch, p.total_tokens, p.max_new_tokens) == (2, 24, 19)
+    assert len(unlaunched) == 2
