@@ -621,6 +621,8 @@ def rope_append_kv(q, k_new, v_new, cos_sin, k_pages, v_pages, page_table, ctx_l
     Tv, v_stride = _token_rows("v_new", v_new, Hkv, D, bf16, dev, batch)
     Hq, q_stride, Tq = 0, 0, T
     if q is not None:
+        if q.dim() < 3:
+            raise ValueError("q [T,Hq,D] or [B,K,Hq,D] expected")
         Hq = q.shape[-2]
         Tq, q_stride = _token_rows("q", q, Hq, D, bf16, dev, batch)
     if Tv != T or Tq != T:

@@ -74,3 +74,13 @@ def test_rows_by_request_name_the_batch(dflash_lib, unlaunched):
     p = unlaunched[1][0]
     assert (p.batch, p.total_tokens, p.max_new_tokens) == (2, 24, 19)
     assert len(unlaunched) == 2
+
+
+def test_rows_of_other_ranks(dflash_lib, unlaunched):
+    d = dflash_lib
+    rows = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    c = cache(rows)
+    for q in (torch.zeros(64, dtype=torch.bfloat16), torch.zeros((), dtype=torch.bfloat16), torch.zeros(2, 64, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="q"):
+            d.rope_append_kv(q, *c["args"][1:], **c["kw"])
+    assert not unlaunched
