@@ -30,7 +30,12 @@ constexpr int kMaxDevices = 64;
 constexpr int kSmemPerSm = 228 * 1024;
 constexpr int kMaxSmemPerCta = 227 * 1024;  // dynamic shared memory one CTA may opt into
 constexpr int kPage8MaxTiles = 1024;   // page-scale form: 128-key tiles per unit, at most
-constexpr double kPage8FillTiles = 4;  // and what a unit's start and end cost, in tile times
+// And what a unit's start and end cost, in tile times: 3 to 11 of them measured
+// (4 us at 4 rows of 128 to 12 us at 128), one number for all.  2 / 4 / 8: 621 /
+// 612 / 638 us (64/16 heads of 64, 24 requests of 1K to 128K), 24.9 / 24.9 / 26.9
+// (8/2, 48 single tokens), 104 / 96 / 94.5 (8/2 of 128, 32 single tokens at 32K);
+// 16 other shapes within 2 %.
+constexpr double kPage8FillTiles = 4;
 
 struct DeviceInfo {
   int sms = 0;

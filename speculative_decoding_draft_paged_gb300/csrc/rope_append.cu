@@ -30,12 +30,13 @@
 // the next one asked for before the maximum of this one is known.  A page slot
 // belongs to the block whose chunk of packed tokens holds its first new row.
 //
-// Measured (bytes over 6.77 TB/s, the rate of a plain copy): to bf16 pages, a
-// prompt of 8191 tokens beside eight short ones, 16/1 heads of 128 69 us, 89 %;
-// 256 blocks of 7 tokens, 64/16 heads of 64 11.0 us, 60 %.  To E4M3 pages, 12
-// prompts of 1 to 4001 tokens, 64/16 heads of 64 106 us, 78 %; 64 blocks of 7
-// tokens, 64/4 heads of 128 6.0 us, 40 %; 256 single tokens, 64/4 heads 5.1 us;
-// one token, 16/1 heads 3.3 us.
+// Measured, replayed in a CUDA graph (bytes over 6.77 TB/s, the rate of a plain
+// copy): to bf16 pages, a prompt of 8191 tokens beside eight short ones, 16/1
+// heads of 128 69 us, 89 %; 256 blocks of 7 tokens, 64/16 heads of 64 11.0 us,
+// 60 %.  To E4M3 pages, 12 prompts of 1 to 4001 tokens, 64/16 heads of 64 107 us,
+// 77 %; 64 blocks of 7 tokens, 64/4 heads of 128 6.4 us, 38 %; 256 single tokens,
+// 64/4 heads 5.1 us; one token, 16/1 heads 3.3 us.  A call from Python in a loop
+// takes 21 to 25 us where the kernel takes less.
 
 #include <cuda_runtime.h>
 

@@ -60,7 +60,7 @@
 // kernel; the combine kernel merges the units.
 // Warps: 4 TG NG softmax warps, then the K producer, the V producer, the QK^T
 // issuer and the PV issuer.  A tile's softmax is a chain (score load, vote,
-// exponentials, stores, fence) of 1500 to 2200 cycles, against the 700
+// exponentials, stores, fence) of 1400 to 2600 cycles, against the 700
 // (D = 64) or 1400 (D = 128) that its codes take from HBM, so tiles have to
 // overlap: up to 32 rows by two or three CTAs on an SM, at 48 and 64 by TG = 2
 // tile groups of four warps (quadrant = warp % 4) that take tiles tg, tg + TG,
@@ -73,14 +73,15 @@
 // ran out goes on with whatever it finds up to its group's next vote, where
 // the group stops.
 //
-// Measured (bytes: codes, scales, tables and rows over 6.77 TB/s, the rate of
-// a plain copy): 24 requests of 1K to 128K keys, 64/16 heads of 64, 7 tokens
-// 599 us, 78 % of that rate; 32 x 128K keys, 12/2 heads of 64, 7 tokens 264 us,
-// 60 %; 64 requests with a window of 4096, 7 tokens, 64/4 heads of 128 95 us,
-// 44 %; 48 requests of 1 to 9001 keys, 8/2 heads of 64, single tokens 21 us,
-// 39 %.  From 48 rows on the chain bounds it, not the bytes: two or three
-// warps a scheduler issue in two thirds of the cycles, and a call pays about
-// 9 us (112 rows) before its first and behind its last full-speed tile.
+// Measured, replayed in a CUDA graph (bytes: codes, scales, tables and rows over
+// 6.77 TB/s, the rate of a plain copy): 24 requests of 1K to 128K keys, 64/16
+// heads of 64, 7 tokens 608 us, 77 % of that rate; 32 x 128K keys, 12/2 heads of
+// 64, 7 tokens 277 us, 57 %; 64 requests with a window of 4096, 7 tokens, 64/4
+// heads of 128 103 us, 41 %; 48 requests of 1 to 9001 keys, 8/2 heads of 64,
+// single tokens 21 us, 39 %.  From 48 rows on the chain bounds it, not the bytes:
+// two or three warps a scheduler issue in two thirds of the cycles, and a unit
+// pays 7 to 12 us before its first and behind its last full-speed tile (112 rows
+// of 128 10.5; up to 32 rows 4 to 7, shared by the CTAs of an SM).
 
 #include <cuda_runtime.h>
 
@@ -118,16 +119,16 @@ enum : uint8_t { kRowTaken, kRowPutOff, kRowDone };  // of a pass over the unit
 constexpr uint32_t kP8Apart = 6;         // powers of two between the largest queries of rows taken together
 
 // Tile and row groups, CTAs per SM and ring stages by head dim and padded rows.
-// Measured, one side against the other:
-//   CTAs per SM, 16 rows: 3 / 2 / 1 at D = 64 20.8 / 21.6 / 26.5 us, 2 / 1 at
-//   D = 128 24.5 / 27.3 (48 requests of 1 to 9001 keys, 8/2 heads; at D = 128
+// Measured, one side against the other, inputs not in L2:
+//   CTAs per SM, 16 rows: 3 / 2 / 1 at D = 64 25.4 / 26.4 / 38.2 us, 2 / 1 at
+//   D = 128 30.0 / 40.2 (48 requests of 1 to 9001 keys, 8/2 heads; at D = 128
 //   shared memory ends at 2).
-//   32 rows: 2 / 1 343 / 505 us at D = 64 (24 requests of 1K to 64K keys, 64/16
-//   heads, 7 tokens), 273 / 318 at D = 128 (to 32K); two to four tile groups in
+//   32 rows: 2 / 1 351 / 522 us at D = 64 (24 requests of 1K to 64K keys, 64/16
+//   heads, 7 tokens), 278 / 329 at D = 128 (to 32K); two to four tile groups in
 //   one CTA instead were slower, too.
-//   Tile groups, 48 rows: 2 / 1 264 / 350 us (D = 64, 32 x 128K keys, 12/2
+//   Tile groups, 48 rows: 2 / 1 281 / 377 us (D = 64, 32 x 128K keys, 12/2
 //   heads, 7 tokens); three have no registers left and were slower.  64 rows:
-//   2 / 1 77 / 95 us at D = 128, 70 / 87 at D = 64 (64 requests, window 4096,
+//   2 / 1 77 / 84 us at D = 128, 71 / 81 at D = 64 (64 requests, window 4096,
 //   64/4 heads, 4 tokens).
 //   Above 64 rows a thread holds its scores and sums of RP / 2 rows: more do
 //   not fit its registers, nor a second accumulator the tensor memory.
@@ -259,7 +260,8 @@ __device__ __forceinline__ float sum8(float (&v)[8], int lane) {
 // f16 holds P <= 2^8 with 11 bits; hi is its nearest E4M3 value, and
 // 32 (P - hi) is exact in f16 and at most 2^8.  (P as one f16 operand, with the
 // value codes widened to f16 in shared memory, saves these conversions, but the
-// widening lengthens the chain: 119 us against 110 at 112 rows.)
+// widening lengthens the chain: 8 % at 112 rows, 119 us against 110 when that was
+// this form's time.)
 __device__ __forceinline__ void split_p4(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
   const uint32_t h01 = pack_f16x2(p0, p1), h23 = pack_f16x2(p2, p3);
   asm("{\n\t.reg .b16 a, b, c, d;\n\t.reg .b32 x, y, u, v, k, n;\n\t"
@@ -727,8 +729,9 @@ __device__ __forceinline__ bool unit_pass(const AttnArgs& a, const float* __rest
       uint32_t x[NR];
       load_scores<NR>(lane_addr + buf * RP + row0, x);
       // y = t + n.  The page's log2 ws joins each row's bias in registers: put
-      // together in shared memory, one lane a row, it took 2 to 4 % longer (64/4
-      // window 99.1 against 95.2 us, 64/16 ragged 607 against 599).
+      // together in shared memory, one lane a row, it took 1 to 4 % longer (64/4
+      // window 99.1 against 95.2 us, 64/16 ragged 607 against 599, of an earlier
+      // form).
       const float4 sc = scale_ring[entry * 8 + page_of_key];
       tc_fence_before();
       __syncwarp();
